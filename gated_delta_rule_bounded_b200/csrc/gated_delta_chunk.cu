@@ -160,7 +160,7 @@ __device__ __forceinline__ void store_neg(unsigned char* img, int r0, int c0, co
   }
 }
 
-// LO: for the gradients, A's low part too.
+// LO: for the gradients, A's low part in an image of its own.
 template <bool LO>
 __global__ void __launch_bounds__(P_THREADS, 5)
     gated_delta_intra_kernel(GatedDeltaParams p, unsigned char* blocks, int64_t stride, const __grid_constant__ QkMaps maps) {
@@ -278,15 +278,22 @@ __global__ void __launch_bounds__(P_THREADS, 5)
       }
     }
     unsigned char* img = sm + (is_q ? P_A : P_Z);
-    const bool low = LO || !is_q;
+    if (!LO && half > lower) continue;  // A's low part stands there
+    // The low part's image, and its row and first 16-byte piece there. Without LO A's takes the upper right quarters.
+    unsigned char* img_l = img + 8192;
+    int tl = t, cl = 4 * half;
+    if (!LO && is_q) {
+      img_l = sm + gb_low_image(lower, half);
+      tl = lane;
+      cl = 4;
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) split2(__uint_as_float(r[8 * j + 2 * e]), __uint_as_float(r[8 * j + 2 * e + 1]), hi[e], lo[e]);
-      const uint32_t at = sw_chunk(t, 4 * half + j, 0);
-      *reinterpret_cast<uint4*>(img + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      if (low) *reinterpret_cast<uint4*>(img + 8192 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      *reinterpret_cast<uint4*>(img + sw_chunk(t, 4 * half + j, 0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(img_l + sw_chunk(tl, cl + j, 0)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   }
   __syncthreads();
@@ -414,19 +421,21 @@ __global__ void __launch_bounds__(P_THREADS, 5)
 // Kernel S: the recurrence of one (sequence, value head, 128 value columns).
 //
 // Everything is transposed: accumulator lane v, columns t or k, so that a token's scalars scale columns. Per chunk:
-//   P1  (K S)^T = S^T K^T       S^T in two parts from tensor memory: 16 MMAs of N = 64    (then Q S, 8 MMAs, high part only)
+//   P1  (K S)^T = S^T K^T       S^T in two parts from tensor memory: 16 MMAs of N = 64    (then Q S, 16 MMAs)
 //   --  R = V - e^G (K S), in two parts to tensor memory
 //   P2  Z R                     12 MMAs of N = 64, 48, 32 and 16 (Z is strictly lower)
 //   --  delta = R + P2, U = beta delta; e^{G_C - G} U and U in two parts
-//   P3  K^T (...)               8 MMAs of N = 128 into a fresh accumulator; then A U onto the output, 8 MMAs
+//   P3  K^T (...)               8 MMAs of N = 128 into a fresh accumulator; then A U onto the output, 14 MMAs
 //   --  S = e^{G_C} S + P3 in fp32 registers (32 a thread)
-// Q S takes S's high part and A U A's: the output is rounded to bf16 itself, the state sees neither.
-// The chain P1 -> R -> P2 -> U -> P3 -> S is what bounds it: 36 MMAs (1,400 cycles at the pipe's rate), three times
+// The output's products take both parts too (A U: high high, high low and, in 6 MMAs of N = 32, low high): it is to carry its
+// own rounding to bf16 and no other of that size. With high parts alone o was off by 1.4 times as much, and the kernel took
+// 184 us instead of 187.
+// The chain P1 -> R -> P2 -> U -> P3 -> S is what bounds it: 36 MMAs of its own (1,400 cycles at the pipe's rate), three times
 // the 165 cycles from the last MMA to the threads that wait for it, and the threads' passes. So a warp of its own issues
 // the MMAs (one elected thread: an N = 64 MMA leaves every 32 cycles), another feeds two stages by TMA a chunk ahead, and
 // what the chain does not need runs in its gaps: V's loads under P1, the conversion of the previous chunk's output under
 // P2, e^G on this chunk's under P3. MMAs run in the order they are issued, so what a later commit covers needs no barrier
-// of its own. Measured, 4096 tokens x 96 heads: 178 us, 2.75 us a chunk (5,300 cycles, of which the passes issue 3,000);
+// of its own. Measured, 4096 tokens x 96 heads: 187 us, 2.9 us a chunk (of some 5,600 cycles the passes issue 3,000);
 // with the gradients' dumps 195.
 // ---------------------------------------------------------------------------------------------------------------------
 constexpr int S_THREADS = 576, S_COMPUTE = 512;  // 16 warps of passes, one of products, one of loads
@@ -551,6 +560,9 @@ __global__ void __launch_bounds__(S_THREADS, 1)
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
             tc_mma_ts(to, tmem + T_SH + 8 * ks, sdesc(st + L::Q + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024), id64, ks > 0);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            tc_mma_ts(to, tmem + T_SL + 8 * ks, sdesc(st + L::Q + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024), id64, 1);
         }
       }
       __syncwarp();
@@ -619,6 +631,13 @@ __global__ void __launch_bounds__(S_THREADS, 1)
             const uint32_t id = idesc_bf16(64 - 16 * ks, 0, 0), at = st + L::B + GB_AH + ks * (32 + 2048);
             tc_mma_ts(to + 16 * ks, tmem + T_U + 16 * ks, sdesc(at, 16, 1024), id, 1);
             tc_mma_ts(to + 16 * ks, tmem + T_U + 16 * ks + 8, sdesc(at, 16, 1024), id, 1);
+          }
+          // A's low part: of 32 x 32 quarter (h, g) tokens 32 h to the output, tokens 32 g of U.
+#pragma unroll
+          for (int i = 0; i < 6; ++i) {
+            const int h = i > 1, g = i > 3, ks = 2 * g + (i & 1);
+            tc_mma_ts(to + 32 * h, tmem + T_U + 16 * ks, sdesc(st + L::B + gb_low_image(h, g) + 64 + 32 * (i & 1), 16, 1024),
+                      idesc_bf16(32, 0, 0), 1);
           }
           tc_commit(b_d);
         }

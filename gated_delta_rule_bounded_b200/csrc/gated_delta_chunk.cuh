@@ -32,9 +32,12 @@ constexpr int GB_ZL = 8192;       // Z, low part
 constexpr int GB_AH = 16384;      // A, high part
 constexpr int GB_VEC = 24576;     // fp32 [64] each: e^G, e^{G_C - G}, beta, then e^{G_C} and a flag; 1 KB
 constexpr int GB_BYTES = 25600;   // what the prefill reads
-constexpr int GB_AL = 25600;      // A, low part (gradients only)
+constexpr int GB_AL = 25600;      // A, low part (the gradients' blocks)
 constexpr int GB_SUMS = 33792;    // the sums of log2 decays, high [64], low [64] (gradients only)
 constexpr int GB_BYTES_BWD = 34304;
+// Tokens 0-31 by tokens 32-63 of Z's two parts and of A's high part are zero, and no product of the prefill reads them: there,
+// in that order, stand the quarters (0, 0), (1, 0) and (1, 1) of A's low part (the gradients read all of A, zeros too).
+__host__ __device__ constexpr int gb_low_image(int h, int g) { return (h + g) * 8192; }
 constexpr int VEC_E = 0, VEC_REST = 64, VEC_BETA = 128, VEC_ALL = 192, VEC_TINY = 193;  // floats within GB_VEC
 constexpr float GD_TINY = 1e-30f;  // the least |beta| of a token
 

@@ -355,14 +355,15 @@ __global__ void __launch_bounds__(R_THREADS, 1)
 // summed in tensor memory (a fixed order, no atomics). Products with M = 128 lanes, in two groups:
 //   lanes i (token):  dO delta^T and dR delta^T, with delta's two parts as the two halves of the lanes; K Q^T and K K^T
 //   lanes k:          S dO, S dR, dS delta; K^T (dO U^T * D)^T, Q^T (dO U^T * D), K^T X^T, K^T X
-// U = beta delta enters as delta, with beta on the accumulators. Every sum that goes into dg takes split operands; dQ and
-// dK, rounded to bf16, take the high part of the D products.
+// U = beta delta enters as delta, with beta on the accumulators. Every sum takes operands in two parts, those of dQ and dK
+// too: they are to carry their own rounding to bf16 and no other of that size.
 //
 // A unit (chunk, value head) reads 240 KB: S and dS 64 KB each, delta and dR 32 KB each, K, Q and dO. That is what bounds
 // the kernel in the end; one block fills an SM's shared memory, so blocks are persistent, a warp of its own loads, in the
 // order in which the unit before releases its buffers (dS follows S through one buffer), another issues the products, and
-// 16 warps do the passes. Measured, 4096 tokens x 96 heads (6,144 units, 1.8 GB): 424 us, 4.2 TB/s; 18,000 cycles a unit,
-// of which the passes issue 9,700 and shared memory's port takes 14,000. One unit after another on 256 threads: 733 us.
+// 16 warps do the passes. Measured, 4096 tokens x 96 heads (6,144 units, 1.8 GB): 441 us, 4.0 TB/s; some 18,700 cycles a
+// unit, of which the passes issue 9,700 and shared memory's port takes 14,800; 96 value heads over 48: 467 us. With the D
+// products' high parts alone 426 and 440 us, dQ and dK off by 1.4 times as much. One unit after another on 256 threads: 733 us.
 // ---------------------------------------------------------------------------------------------------------------------
 constexpr int G_THREADS = 576, G_COMPUTE = 512;
 constexpr int G_S = 0;               // 64 KB: S's images, then dS's
@@ -370,9 +371,9 @@ constexpr int G_KQ = 65536;          // 32 KB: [64-channel half][K 64 rows ; Q 6
 constexpr int G_DO = 98304;          // 16 KB
 constexpr int G_D = 114688;          // 32 KB: delta^T [v][t] bf16, high then low
 constexpr int G_DR = 147456;         // 32 KB: dR fp32 [t / 4][v][t & 3], then dR^T [v][t] bf16, high then low
-constexpr int G_I = 180224;          // 16 KB: dV's tile [t][v]; an exchange buffer; (dO U^T * D)^T and X^T as [i][t] bf16;
-                                     // dQ's tile [t][k]
-constexpr int G_XB = 196608;         // 16 KB: the other exchange buffer, then dK's tile
+constexpr int G_I = 180224;          // 16 KB: dV's tile [t][v]; an exchange buffer; (dO U^T * D)^T and X^T as [i][t] bf16,
+                                     // high parts; dQ's tile [t][k]
+constexpr int G_XB = 196608;         // 16 KB: the other exchange buffer, the low parts of those, then dK's tile
 constexpr int G_VEC = 212992;        // 1.5 KB: the block's vectors and its sums of log2 decays
 constexpr int G_F = G_VEC + 1536;    // partial sums, floats
 constexpr int GF_X = 0, GF_COL = 256, GF_BETA = 768, GF_Z = 1024, GF_A = 1040;
@@ -584,10 +585,14 @@ __global__ void __launch_bounds__(G_THREADS, 1)
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
           const uint64_t kt = sdesc(sb + G_KQ + ks * 2048, 16384, 1024), qt = sdesc(sb + G_KQ + 8192 + ks * 2048, 16384, 1024);
-          tc_mma(tmem + TG::DQ, kt, sdesc(sb + G_I + ks * 2048, 8192, 1024), id_tt, ks > 0 || (!ONE && u.r));
-          tc_mma(tmem + TG::DK, qt, sdesc(sb + G_I + ks * 32, 16, 1024), id_tn, ks > 0 || (!ONE && u.r));
-          tc_mma(tmem + TG::DK, kt, sdesc(sb + G_I + 8192 + ks * 2048, 8192, 1024), id_tt, 1);
-          tc_mma(tmem + TG::DK, kt, sdesc(sb + G_I + 8192 + ks * 32, 16, 1024), id_tn, 1);
+#pragma unroll
+          for (int lo = 0; lo < 2; ++lo) {
+            const uint32_t img = sb + (lo ? G_XB : G_I), more = lo || ks > 0 || (!ONE && u.r);
+            tc_mma(tmem + TG::DQ, kt, sdesc(img + ks * 2048, 8192, 1024), id_tt, more);
+            tc_mma(tmem + TG::DK, qt, sdesc(img + ks * 32, 16, 1024), id_tn, more);
+            tc_mma(tmem + TG::DK, kt, sdesc(img + 8192 + ks * 2048, 8192, 1024), id_tt, 1);
+            tc_mma(tmem + TG::DK, kt, sdesc(img + 8192 + ks * 32, 16, 1024), id_tn, 1);
+          }
         }
       }
       __syncwarp();
@@ -726,7 +731,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             static_cast<__nv_bfloat16*>(d.dv)[(((int64_t)u.brow * p.T + u.tc0 + t) * p.HV + u.hv(rep)) * p.V + 32 * quad + lane] =
                 __float2bfloat16_rn(0.f);
       float X[16];     // this thread's share of x_t = dg_{t+1} - dg_t at its 16 tokens
-      uint32_t pk[8];  // its row of the images
+      uint32_t pk[8], pl[8];  // its row of the images, two parts
       {
         const float* other = (quad < 2 ? xa : xb) + t0 * 64 + i;
         const float ghi = gh[i], glo = gl[i], b = quad < 2 ? vec[VEC_BETA + i] : -vec[VEC_BETA + i];
@@ -734,10 +739,15 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         float col = 0.f;
 #pragma unroll
         for (int p8 = 0; p8 < 16; p8 += 8) {
-          uint32_t own[8], more[8], inner[8];  // inner: k_i . q_t, or k_i . k_t
+          uint32_t own[8], inner[8];  // inner: k_i . q_t, or k_i . k_t
           tm_ld8(t_own + p8, own);
+          if (ONE && quad >= 2) {
+            tm_ld8(t_own + 64 + p8, inner);
+            tm_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) own[j] = __float_as_uint(__uint_as_float(own[j]) + __uint_as_float(inner[j]));
+          }
           tm_ld8(t_in + p8, inner);
-          if (ONE && quad >= 2) tm_ld8(t_own + 64 + p8, more);
           tm_wait_ld();
 #pragma unroll
           for (int j = 0; j < 8; j += 4) {
@@ -748,7 +758,6 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             for (int e = 0; e < 4; ++e) {
               const int t = t0 + p8 + j + e;
               float x = __uint_as_float(own[j + e]) + other[(p8 + j + e) * 64];
-              if (ONE && quad >= 2) x += __uint_as_float(more[j + e]);
               const float dec = b * ex2((gt[e] - ghi) + (lt[e] - glo));
               const bool keep = t < nv && (quad < 2 ? i <= t : i < t);
               y[e] = keep ? x * dec : 0.f;
@@ -756,8 +765,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
               X[p8 + j + e] = -P;
               col += P;
             }
-            pk[(p8 + j) >> 1] = pack_bf16(y[0], y[1]);
-            pk[((p8 + j) >> 1) + 1] = pack_bf16(y[2], y[3]);
+            split2(y[0], y[1], pk[(p8 + j) >> 1], pl[(p8 + j) >> 1]);
+            split2(y[2], y[3], pk[((p8 + j) >> 1) + 1], pl[((p8 + j) >> 1) + 1]);
           }
         }
         F[GF_COL + 64 * (4 * (quad >> 1) + part) + i] = col;
@@ -765,9 +774,11 @@ __global__ void __launch_bounds__(G_THREADS, 1)
       tc_fence_before();
       named_sync<3, G_COMPUTE>();  // the exchange buffers are read
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        *reinterpret_cast<uint4*>(sm + G_I + (quad < 2 ? 0 : 8192) + sw_chunk(i, 2 * part + j, 0)) =
-            make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t at = (quad < 2 ? 0 : 8192) + sw_chunk(i, 2 * part + j, 0);
+        *reinterpret_cast<uint4*>(sm + G_I + at) = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+        *reinterpret_cast<uint4*>(sm + G_XB + at) = make_uint4(pl[4 * j], pl[4 * j + 1], pl[4 * j + 2], pl[4 * j + 3]);
+      }
       fence_async_smem();
       named_arrive<2, G_COMPUTE + 32>();
       {  // <S, dS>

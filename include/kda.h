@@ -401,10 +401,10 @@ int kda_bounded_decay_backward(const float* logits, const float* A_log, float g_
  * in [16, 256] (the gradients: 16, 32, 64 or 128); B*T*HV and 16*N*HV below
  * 2^31.
  *
- * The state is fp32 and every product that leads to it is carried to about 16
- * bits beyond the inputs' own (bf16 operands in two parts where an operand is
- * not a bf16 input itself), so final states, d_initial_state, dg and dbeta
- * are good to about 5e-6 of their norm; o, dq, dk and dv round to `dtype`.
+ * The state is fp32 and every product takes its operands to about 16 bits (two
+ * bf16 parts where an operand is not a bf16 input itself), so final states,
+ * d_initial_state, dg and dbeta are good to about 5e-6 of their norm, and o, dq,
+ * dk and dv to that before they round to `dtype`.
  *
  * kda_gated_delta_prefill runs bf16 inputs with K <= 128 in chunks of 64 tokens
  * on the tensor cores when given a workspace (as many bytes as

@@ -49,3 +49,23 @@ def test_outputs(B, T, H, HV, K, V, cuts, q_scale):
     assert not kda.device_status()
     a, b = (0, T) if cuts is None else (cuts[0], cuts[-1])
     rounded(got[:, a:b], o[:, a:b], "o")
+
+
+GRADS = [  # B, T, H, HV, K, V, packed offsets
+    (1, 64, 1, 2, 128, 128, None), (2, 200, 2, 2, 128, 128, None), (1, 333, 1, 3, 128, 128, None), (1, 97, 2, 2, 64, 32, None),
+    (1, 300, 2, 4, 64, 64, (3, 70, 70, 71, 200, 299)), (1, 1500, 1, 1, 64, 64, None),
+]
+
+
+@pytest.mark.parametrize("B,T,H,HV,K,V,cuts", GRADS)
+def test_gradients(B, T, H, HV, K, V, cuts):
+    n = B if cuts is None else len(cuts) - 1
+    d = ref.inputs(B, T, H, HV, K, V, BF, seed=T + V, n_states=n)
+    want = ref.gradients(d["q"], d["k"], d["v"], d["g"], d["beta"], d["s0"], d["d_o"], d["d_sf"], cuts)
+    x = {m: t.to(DEV) for m, t in d.items()}
+    cu = None if cuts is None else torch.tensor(cuts, device=DEV, dtype=torch.int32)
+    got = kda.gated_delta_backward(x["q"], x["k"], x["v"], x["g"], x["beta"], x["s0"], x["d_o"], x["d_sf"], cu)
+    torch.cuda.synchronize()
+    assert not kda.device_status()
+    for m in ("dq", "dk", "dv"):
+        rounded(got[m], want[m], m)

@@ -800,8 +800,9 @@ def gated_delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: t
     _state_ok(d_final_state, "d_final_state", shape, dev)
     new = torch.zeros if cu is not None else torch.empty  # tokens outside every sequence: zero
     out = {"dq": new(q.shape, device=dev, dtype=q.dtype), "dk": new(q.shape, device=dev, dtype=q.dtype),
-           "dv": new(v.shape, device=dev, dtype=q.dtype), "dg": new(g.shape, device=dev),
-           "dbeta": new(g.shape, device=dev), "d_initial_state": torch.empty(shape, device=dev)}
+           "dv": new(v.shape, device=dev, dtype=q.dtype), "dg": new(g.shape, device=dev, dtype=torch.float32),
+           "dbeta": new(g.shape, device=dev, dtype=torch.float32),
+           "d_initial_state": torch.empty(shape, device=dev, dtype=torch.float32)}
     if workspace is None:
         need = gated_delta_backward_workspace_bytes(B, T, H, HV, K, V, n_seq, q.dtype)
         workspace = torch.empty(max(need, 16), device=dev, dtype=torch.uint8)

@@ -509,9 +509,10 @@ def scan_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gate: torch
         if t is not None and t.shape != (N, H, K, V):
             raise ValueError(f"{n} must be [{N},{H},{K},{V}]")
     new = torch.zeros if cu_seqlens is not None else torch.empty
-    out = {"dq": new(B, T, H, K, device=dev), "dk": new(B, T, H, K, device=dev),
-           "dv": new(B, T, H, V, device=dev), "dgate": new(B, T, H, K, device=dev),
-           "dbeta": new(B, T, H, device=dev), "d_initial_state": torch.empty(N, H, K, V, device=dev)}
+    f32s = dict(device=dev, dtype=torch.float32)
+    out = {"dq": new(B, T, H, K, **f32s), "dk": new(B, T, H, K, **f32s), "dv": new(B, T, H, V, **f32s),
+           "dgate": new(B, T, H, K, **f32s), "dbeta": new(B, T, H, **f32s),
+           "d_initial_state": torch.empty(N, H, K, V, **f32s)}
     lib = load_library()
     n = ctypes.c_size_t(0)
     _check("kda_scan_backward_workspace_bytes",
@@ -565,9 +566,10 @@ def scan_backward_chunked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gat
         if t is not None and t.shape != (N, H, K, V):
             raise ValueError(f"{n} must be [{N},{H},{K},{V}]")
     new = torch.zeros if cu_seqlens is not None else torch.empty  # tokens outside every sequence: zero
-    out = {"dq": new(B, T, H, K, device=dev), "dk": new(B, T, H, K, device=dev),
-           "dv": new(B, T, H, V, device=dev), "dgate": new(B, T, H, K, device=dev),
-           "dbeta": new(B, T, H, device=dev), "d_initial_state": torch.empty(N, H, K, V, device=dev)}
+    f32s = dict(device=dev, dtype=torch.float32)
+    out = {"dq": new(B, T, H, K, **f32s), "dk": new(B, T, H, K, **f32s), "dv": new(B, T, H, V, **f32s),
+           "dgate": new(B, T, H, K, **f32s), "dbeta": new(B, T, H, **f32s),
+           "d_initial_state": torch.empty(N, H, K, V, **f32s)}
     lib = load_library()
     need = chunked_backward_workspace_bytes(B, T, H, K, V, n_seq)
     if workspace is None:
@@ -600,7 +602,7 @@ def bounded_decay_backward(logits: torch.Tensor, A_log: torch.Tensor, g_min: flo
     z = logits.to(torch.float32).contiguous()
     dg = d_log_decay.to(device=z.device, dtype=torch.float32).contiguous()
     A = A_log.to(device=z.device, dtype=torch.float32).contiguous()
-    dz, dA = torch.empty_like(z), torch.empty(H, device=z.device)
+    dz, dA = torch.empty_like(z), torch.empty(H, device=z.device, dtype=torch.float32)
     _check("kda_bounded_decay_backward", load_library().kda_bounded_decay_backward(
         z.data_ptr(), A.data_ptr(), float(g_min), dg.data_ptr(), B, T, H, K, dz.data_ptr(), dA.data_ptr(),
         _stream(z.device)))

@@ -61,3 +61,20 @@ def test_layer_norm(other_default, dtype):
     assert y.dtype == dtype and mean.dtype == rstd.dtype == F
     out = kda.layer_norm_backward(x, x, w, mean, rstd)
     assert out["dx"].dtype == dtype and out["dweight"].dtype == out["dbias"].dtype == F
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_channel_decays(other_default, packed):
+    q, gate, beta = tokens(), tokens(dtype=F), torch.zeros(1, 70, 2, dtype=F)
+    cu = torch.tensor([0, 30, 70], dtype=torch.int32) if packed else None
+    n = 2 if packed else 1
+    for call in (kda.scan_backward, kda.scan_backward_chunked):
+        out = call(q, q, q, gate, beta, None, q, None, cu)
+        for m, x in (("dq", q), ("dk", q), ("dv", q), ("dgate", q), ("dbeta", beta)):
+            assert out[m].shape == x.shape and out[m].dtype == F, (call, m)
+        assert out["d_initial_state"].shape == (n, 2, 128, 128) and out["d_initial_state"].dtype == F
+    o, state = kda.prefill(q, q, q, gate, beta, None, cu)
+    assert o.dtype == BF and state.dtype == F
+    dz, dA = kda.bounded_decay_backward(gate, torch.zeros(2, dtype=F), -5.0, gate)
+    assert dz.dtype == F and dA.dtype == F
+    assert kda.bounded_decay(gate, torch.zeros(2, dtype=F)).dtype == F

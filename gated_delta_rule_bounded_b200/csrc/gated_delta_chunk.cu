@@ -1106,8 +1106,14 @@ size_t gated_delta_chunk_bytes(int64_t B, int64_t T, int64_t H, int64_t HV, int6
   // Measured, chunked and token by token: 32 heads, 1 token 15 and 3.9 us, 32 tokens 15 and 11.5, 48 tokens 15.2 and 15.3;
   // 96 heads, 16 tokens 15.4 and 14.2, 32 tokens 15.4 and 24; 8 x 96 heads, 8 tokens 66 and 53; 64 x 32 heads, 4 tokens 170
   // and 99, 16 tokens 174 and 213.
-  const double warps = (double)(n_seq > 0 ? n_seq : B) * (double)HV * (double)V * 4 / 32 / (4 * GD_SMS);
-  if (T <= 8 || (double)T * std::max(warps, 1.0) <= 44) return 0;
+  // Packed, T counts all tokens, and one sequence may have them all: the warps are one sequence's. Every further sequence costs
+  // its states' way in and out, 5 us for as many chains as SMs, and the chunked kernels a chunk too, 12 us: the difference is
+  // worth 24 tokens at least. Measured, 32 heads, chunked and token by token: 16 sequences of 2 tokens 49 and 22 us, 40 of one
+  // 119 and 47, 40 of 8 tokens 121 and 89 (132 where one has all but 39), 40 of 16 tokens 124 and 135; 96 heads, 64 of 4
+  // tokens 529 and 296, 64 of 16 548 and 632.
+  const double warps = (double)(n_seq > 0 ? 1 : B) * (double)HV * (double)V * 4 / 32 / (4 * GD_SMS);
+  const double further = (double)n_seq * (double)HV * (double)((V + VT - 1) / VT) / GD_SMS;
+  if (T <= 8 || (double)T * std::max(warps, 1.0) <= std::max(44.0, 24 * further)) return 0;
   return (split ? gd_split_shape(B, T, HV, K, V, n_seq, false).bytes : 0) + (size_t)gd_slots(B, T, n_seq) * HV * GB_BYTES;
 }
 

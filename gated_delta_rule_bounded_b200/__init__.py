@@ -154,7 +154,11 @@ def _rowwise(t: torch.Tensor) -> torch.Tensor:
     es = t.element_size()
     aligned = t.data_ptr() % 16 == 0 and all(
         (s * es) % 16 == 0 or n <= 1 for s, n in zip(t.stride()[:-1], t.shape[:-1]))
-    return t if aligned else t.contiguous()
+    if aligned:
+        return t
+    if t.is_contiguous():  # only its base can be moved
+        return t.clone() if t.data_ptr() % 16 else t
+    return t.contiguous()
 
 
 def _strides4(t: torch.Tensor) -> Strides:

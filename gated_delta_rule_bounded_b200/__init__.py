@@ -636,6 +636,11 @@ def _same_device(device: torch.device, **tensors):
             raise ValueError(f"{name} is on {t.device}, q on {device}")
 
 
+def _unexpanded(t: torch.Tensor) -> torch.Tensor:
+    """The chunked kernels read by TMA, which takes no stride of zero (an expanded tensor): a copy of such a one."""
+    return t.contiguous() if 0 in t.stride() and any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)) else t
+
+
 def _gated_delta_inputs(q, k, v, g, beta, dims):
     """Checks what the three scan calls share; returns q, k, v with aligned rows."""
     _cuda(q, "q")
@@ -731,6 +736,8 @@ def gated_delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: to
     elif use_workspace:
         need = gated_delta_prefill_workspace_bytes(B, T, H, HV, K, V, n_seq, q.dtype)
         workspace = torch.empty(need, device=dev, dtype=torch.uint8) if need else None
+    if workspace is not None:
+        q, k, v = map(_unexpanded, (q, k, v))
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     layout = Layout(*(t.stride()[:3] for t in (q, k, v, g, beta, out)))
     with _on(dev):
@@ -798,8 +805,7 @@ def gated_delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: t
     if d_o.shape != v.shape or d_o.dtype != v.dtype:
         raise ValueError("d_o must have v's shape and dtype")
     d_o = _rowwise(d_o)
-    # The kernels read by TMA, which takes no stride of zero (an expanded tensor).
-    q, k, v, d_o = (x.contiguous() if any(s == 0 and m > 1 for s, m in zip(x.stride(), x.shape)) else x for x in (q, k, v, d_o))
+    q, k, v, d_o = map(_unexpanded, (q, k, v, d_o))
     cu, cu_ptr, n_seq, N = _packed(cu_seqlens, B, dev)
     shape = (N, HV, K, V)
     _state_ok(initial_state, "initial_state", shape, dev)

@@ -410,7 +410,8 @@ int kda_bounded_decay_backward(const float* logits, const float* A_log, float g_
  * on the tensor cores when given a workspace (as many bytes as
  * kda_gated_delta_prefill_workspace_bytes says; n_seq 0 without cu_seqlens; 0
  * bytes where no path uses it); without, for a few tokens, and for every other
- * input, token by token.
+ * input (q, k or v with a stride of zero over an extent above one among them),
+ * token by token.
  * In chunks a beta of magnitude below 1e-30 counts as 1e-30 (dv is zero there),
  * and an infinity or NaN in a token may reach earlier tokens of its chunk, of the
  * same sequence and value head. Few long sequences run in segments side by side,

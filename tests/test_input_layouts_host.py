@@ -74,3 +74,27 @@ def test_every_call_gets_rows_on_boundaries(library, dtype):
             assert x % 16 == 0, name
     with pytest.raises(ValueError):  # what the call writes is the caller's: not copied, refused
         kda.gated_delta_prefill(q, q, v, g, g, out=shifted(1, 70, 4, 64, dtype=dtype))
+
+
+def strides(layout, name):
+    s = getattr(layout._obj, name)
+    return (s.b, s.t, s.h)
+
+
+@pytest.mark.parametrize("which", ["q", "k", "v"])
+def test_expanded_inputs_run_in_chunks(library, which):
+    """A stride of zero would send the prefill token by token: the chunked kernels read by TMA, which takes none."""
+    x = {"q": torch.randn(2, 100, 2, 64).to(BF), "k": torch.randn(2, 100, 2, 64).to(BF), "v": torch.randn(2, 100, 4, 64).to(BF)}
+    x[which] = x[which][:, :, :1].expand_as(x[which])
+    g = torch.zeros(2, 100, 4)
+    kda.gated_delta_prefill(x["q"], x["k"], x["v"], g, g)
+    name, args = library.calls.pop()
+    assert name == "kda_gated_delta_prefill" and args[18] and 0 not in strides(args[-5], which)
+    # Token by token (no workspace, or fp32) such strides are read as they are.
+    kda.gated_delta_prefill(x["q"], x["k"], x["v"], g, g, use_workspace=False)
+    assert strides(library.calls.pop()[1][-5], which)[2] == 0
+    kda.gated_delta_prefill(x["q"].float(), x["k"].float(), x["v"].float(), g, g)
+    assert library.calls.pop()[1][18] is None
+    # One token row and one head have no stride that counts.
+    kda.gated_delta_prefill(x["q"][:1, :, :1], x["k"][:1, :, :1], x["v"][:1, :, :1], g[:1, :, :1], g[:1, :, :1])
+    assert library.calls.pop()[1][0 if which == "q" else 1 if which == "k" else 2] == x[which].data_ptr()

@@ -883,10 +883,11 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
 
 
 def layer_norm_backward(d_y: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
-                        rstd: torch.Tensor, *, weight_grads: bool = True) -> dict:
+                        rstd: torch.Tensor, *, bias: Optional[torch.Tensor] = None, weight_grads: bool = True) -> dict:
     """Gradients of ``layer_norm`` (``kda_layer_norm_backward``): ``dx`` in x's dtype, and the sums over rows
-    ``dweight`` and ``dbias`` in the weight's dtype (None without a weight, or with ``weight_grads=False``).
-    ``mean`` and ``rstd`` are the forward call's."""
+    ``dweight`` and ``dbias`` in the weight's dtype. ``mean`` and ``rstd`` are the forward call's. After a call
+    with a bias and no weight give its ``bias``: ``dbias`` then has its dtype. ``dweight`` is None without a
+    weight, ``dbias`` without either, both with ``weight_grads=False``."""
     _cuda(x, "x")
     code = _dtype_code(x.dtype)
     for t, n in ((d_y, "d_y"), (mean, "mean"), (rstd, "rstd")):
@@ -897,7 +898,10 @@ def layer_norm_backward(d_y: torch.Tensor, x: torch.Tensor, weight: Optional[tor
         raise ValueError("d_y must have x's shape and dtype")
     if mean.shape != x.shape[:-1] or rstd.shape != x.shape[:-1] or mean.dtype != torch.float32 or rstd.dtype != torch.float32:
         raise ValueError("mean and rstd must be the forward call's fp32 [...] tensors")
-    weight = _norm_weight(weight, "weight", x)
+    weight, bias = _norm_weight(weight, "weight", x), _norm_weight(bias, "bias", x)
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must share one dtype")
+    wt = weight if weight is not None else bias
     (rows, n_rows, stride), (grads, _, g_stride) = _rows2d(x), _rows2d(d_y)
     mean, rstd = mean.contiguous(), rstd.contiguous()
     dev = x.device
@@ -905,14 +909,14 @@ def layer_norm_backward(d_y: torch.Tensor, x: torch.Tensor, weight: Optional[tor
     dweight = dbias = workspace = None
     ws_bytes = 0
     lib = load_library()
-    if weight is not None and weight_grads:
-        dweight, dbias = torch.empty_like(weight), torch.empty_like(weight)
+    if wt is not None and weight_grads:
+        dweight, dbias = None if weight is None else torch.empty_like(wt), torch.empty_like(wt)
         ws_bytes = _workspace_bytes("kda_layer_norm_backward_workspace_bytes", n_rows, x.shape[-1])
         workspace = torch.empty(max(ws_bytes, 16), device=dev, dtype=torch.uint8)
     with _on(dev):
         _check("kda_layer_norm_backward", lib.kda_layer_norm_backward(
             grads.data_ptr(), g_stride, rows.data_ptr(), stride, code, _ptr(weight),
-            code if weight is None else _dtype_code(weight.dtype), mean.data_ptr(), rstd.data_ptr(), n_rows,
+            code if wt is None else _dtype_code(wt.dtype), mean.data_ptr(), rstd.data_ptr(), n_rows,
             x.shape[-1], dx.data_ptr(), _ptr(dweight), _ptr(dbias), _ptr(workspace), ws_bytes, _stream(dev)))
     return {"dx": dx, "dweight": dweight, "dbias": dbias}
 

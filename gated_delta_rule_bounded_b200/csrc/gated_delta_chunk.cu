@@ -160,7 +160,7 @@ __device__ __forceinline__ void store_neg(unsigned char* img, int r0, int c0, co
   }
 }
 
-// LO: for the gradients, A's low part in an image of its own.
+// LO: for the gradients, A's low part in an image of its own and no write strength of zero.
 template <bool LO>
 __global__ void __launch_bounds__(P_THREADS, 5)
     gated_delta_intra_kernel(GatedDeltaParams p, unsigned char* blocks, int64_t stride, const __grid_constant__ QkMaps maps) {
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(P_THREADS, 5)
   }
   if (warp == 1) tm_alloc(smem_u32(tslot), 64);
   if (warp == 3) {
-    gd_decays(p, hv, tc0, brow, nv, lane, vec, gh, gl);
+    gd_decays(p, hv, tc0, brow, nv, lane, LO ? GD_TINY : 0.f, vec, gh, gl);
     __syncwarp();
     const float c = ex2((gh[31] - gh[lane]) + (gl[31] - gl[lane]));
     gl[64 + lane] = c;

@@ -39,7 +39,7 @@ constexpr int GB_BYTES_BWD = 34304;
 // in that order, stand the quarters (0, 0), (1, 0) and (1, 1) of A's low part (the gradients read all of A, zeros too).
 __host__ __device__ constexpr int gb_low_image(int h, int g) { return (h + g) * 8192; }
 constexpr int VEC_E = 0, VEC_REST = 64, VEC_BETA = 128, VEC_ALL = 192, VEC_TINY = 193;  // floats within GB_VEC
-constexpr float GD_TINY = 1e-30f;  // the least |beta| of a token
+constexpr float GD_TINY = 1e-30f;  // the least |beta| of a token in the gradients
 
 __device__ __forceinline__ int64_t gd_slot_base(const GatedDeltaParams& p, int n, int64_t t0) {
   return p.cu ? t0 / C + n : (int64_t)n * ((p.T + C - 1) / C);
@@ -262,9 +262,10 @@ __device__ __forceinline__ void tm_dealloc(uint32_t tmem, uint32_t cols) {
 }
 
 // One warp: the running sums of a chunk's log2 decays, in fp64 (lane l holds tokens 2l and 2l + 1), as two fp32 parts
-// in gh and gl, and the block's vectors. Tokens past the sequence's end get no decay and no write strength.
+// in gh and gl, and the block's vectors. Tokens past the sequence's end get no decay and no write strength. Strengths of a
+// magnitude below `least` count as that.
 __device__ __forceinline__ void gd_decays(const GatedDeltaParams& p, int hv, int64_t tc0, int64_t brow, int nv, int lane,
-                                          float* vec, float* gh, float* gl) {
+                                          float least, float* vec, float* gh, float* gl) {
   const float* g = p.g + brow * p.gs[0] + hv * p.gs[2] + tc0 * p.gs[1];
   const float* beta = p.beta + brow * p.bs[0] + hv * p.bs[2] + tc0 * p.bs[1];
   double x[2];
@@ -275,10 +276,10 @@ __device__ __forceinline__ void gd_decays(const GatedDeltaParams& p, int hv, int
     x[e] = t < nv ? (double)g[t * p.gs[1]] * 1.4426950408889634 : 0.0;
     // Far below what 2^x can hold, so that g = -inf keeps the sums' differences defined (and NaN stays NaN).
     x[e] = x[e] < -1e4 ? -1e4 : x[e];
-    // A write strength of zero becomes one too small to matter, so that dY = dR / beta is defined; VEC_TINY tells.
+    // In the gradients a write strength of zero becomes one too small to matter, so that dY = dR / beta is defined; VEC_TINY tells.
     const float b = t < nv ? beta[t * p.bs[1]] : 0.f;
-    const bool small = t < nv && fabsf(b) < GD_TINY;
-    vec[VEC_BETA + t] = small ? GD_TINY : b;
+    const bool small = t < nv && fabsf(b) < least;
+    vec[VEC_BETA + t] = small ? least : b;
     tiny |= small;
   }
   double sum = x[0] + x[1];

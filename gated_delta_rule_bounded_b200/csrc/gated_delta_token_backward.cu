@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(TB_THREADS, 1)
     rows(sm.o, static_cast<const float*>(d.d_o) + brow * p.os[0] + tc0 * p.os[1] + hv * p.os[2], p.os[1], V);
     rows(sm.c, rev.rows + first * V, (int64_t)p.HV * V, V);
     rows(sm.delta, fwd.rows + first * V, (int64_t)p.HV * V, V);
-    if (warp == 0) gd_decays(p, hv, tc0, brow, nv, lane, sm.vec, sm.gh, sm.gl);
+    if (warp == 0) gd_decays(p, hv, tc0, brow, nv, lane, 0.f, sm.vec, sm.gh, sm.gl);
     if (tid >= 64 && tid < 64 + C)
       sm.beta[tid - 64] = tid - 64 < nv ? p.beta[brow * p.bs[0] + hv * p.bs[2] + (tc0 + tid - 64) * p.bs[1]] : 0.f;
     __syncthreads();

@@ -412,14 +412,14 @@ int kda_bounded_decay_backward(const float* logits, const float* A_log, float g_
  * bytes where no path uses it); without, for a few tokens, and for every other
  * input (q, k or v with a stride of zero over an extent above one among them),
  * token by token.
- * In chunks a beta of magnitude below 1e-30 counts as 1e-30 (dv is zero there),
- * and an infinity or NaN in a token may reach earlier tokens of its chunk, of the
- * same sequence and value head. Few long sequences run in segments side by side,
- * joined through their maps of the state. That takes up to 40 MB (the gradients
- * 50) of the bytes asked for, more with more heads; a workspace that lacks them,
- * for instance one made for a longer call, runs every sequence whole. Which it is
- * follows from the sizes, cu_seqlens and the workspace's size alone, so equal
- * calls give equal bits.
+ * In the chunked gradients a beta of magnitude below 1e-30 counts as 1e-30 (dv is
+ * zero there). In chunks an infinity or NaN in a token may reach earlier tokens of
+ * its chunk, of the same sequence and value head. Few long sequences run in
+ * segments side by side, joined through their maps of the state. That takes up to
+ * 40 MB (the gradients 50) of the bytes asked for, more with more heads; a
+ * workspace that lacks them, for instance one made for a longer call, runs every
+ * sequence whole. Which it is follows from the sizes, cu_seqlens and the
+ * workspace's size alone, so equal calls give equal bits.
  *
  * kda_gated_delta_decode_step: one token (q, k [B,H,K], v, o [B,HV,V], g, beta
  * [B,HV]; t strides ignored), state [B,HV,K,V] updated in place.

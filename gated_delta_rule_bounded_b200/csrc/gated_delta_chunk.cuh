@@ -39,7 +39,9 @@ constexpr int GB_BYTES_BWD = 34304;
 // in that order, stand the quarters (0, 0), (1, 0) and (1, 1) of A's low part (the gradients read all of A, zeros too).
 __host__ __device__ constexpr int gb_low_image(int h, int g) { return (h + g) * 8192; }
 constexpr int VEC_E = 0, VEC_REST = 64, VEC_BETA = 128, VEC_ALL = 192, VEC_TINY = 193;  // floats within GB_VEC
-constexpr float GD_TINY = 1e-30f;  // the least |beta| of a token in the gradients
+// The least |beta| of a token in the gradients: 2^-66, 1e-20 of what the other tokens write, and dR = beta dY stays a normal
+// number, and its two parts too, for dY down to 2^-51 (with 1e-30 dbeta lost digits from gradients of 1e-11 down).
+constexpr float GD_TINY = 0x1p-66f;
 
 __device__ __forceinline__ int64_t gd_slot_base(const GatedDeltaParams& p, int n, int64_t t0) {
   return p.cu ? t0 / C + n : (int64_t)n * ((p.T + C - 1) / C);

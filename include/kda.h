@@ -412,7 +412,7 @@ int kda_bounded_decay_backward(const float* logits, const float* A_log, float g_
  * bytes where no path uses it); without, for a few tokens, and for every other
  * input (q, k or v with a stride of zero over an extent above one among them),
  * token by token.
- * In the chunked gradients a beta of magnitude below 1e-30 counts as 1e-30 (dv is
+ * In the chunked gradients a beta of magnitude below 2^-66 counts as 2^-66 (dv is
  * zero there). In chunks an infinity or NaN in a token may reach earlier tokens of
  * its chunk, of the same sequence and value head. Few long sequences run in
  * segments side by side, joined through their maps of the state. That takes up to

@@ -255,6 +255,15 @@ static int check_norm(const char* fn, kda_dtype dtype, kda_dtype weight_dtype, i
   return KDA_OK;
 }
 
+// Whether `rows` contiguous rows at y meet the rows of x, `stride` elements apart, anywhere but where y is x.
+static bool rows_clash(const void* y, const void* x, int64_t stride, int64_t rows, int64_t D, kda_dtype dt) {
+  const int64_t es = dt == KDA_F32 ? 4 : 2, width = D * es, step = stride * es;
+  if (y == x && (stride == D || rows == 1)) return false;
+  if (!overlap(y, (size_t)(rows * width), x, (size_t)((rows - 1) * step + width))) return false;
+  const int64_t off = static_cast<const char*>(y) - static_cast<const char*>(x);
+  return !(step > width && off > 0 && off % step >= width && off % step + rows * width <= step);  // between two rows
+}
+
 static bool aligned_to(const void* p, kda_dtype dt) { return reinterpret_cast<uintptr_t>(p) % (dt == KDA_F32 ? 4 : 2) == 0; }
 
 int kda_layer_norm(const void* x, int64_t x_stride, kda_dtype dtype, const void* weight, const void* bias,
@@ -269,6 +278,7 @@ int kda_layer_norm(const void* x, int64_t x_stride, kda_dtype dtype, const void*
   if (!aligned_to(x, dtype) || !aligned_to(y, dtype) || !aligned_to(weight, weight_dtype) ||
       !aligned_to(bias, weight_dtype) || !aligned_to(mean, KDA_F32) || !aligned_to(rstd, KDA_F32))
     return fail(KDA_ERR_UNSUPPORTED, "%s: misaligned pointer", fn);
+  if (rows_clash(y, x, x_stride, rows, D, dtype)) return fail(KDA_ERR_INVALID_ARG, "%s: y and x overlap partially", fn);
   kda::LayerNormParams p{};
   p.x = x;
   p.weight = weight;
@@ -312,6 +322,8 @@ int kda_layer_norm_backward(const void* d_y, int64_t d_y_stride, const void* x, 
   }
   if (!d_y || !x || !mean || !rstd || !dx) return fail(KDA_ERR_INVALID_ARG, "%s: null pointer", fn);
   if (x_stride < 0 || d_y_stride < 0) return fail(KDA_ERR_INVALID_ARG, "%s: negative stride", fn);
+  if (rows_clash(dx, x, x_stride, rows, D, dtype) || rows_clash(dx, d_y, d_y_stride, rows, D, dtype))
+    return fail(KDA_ERR_INVALID_ARG, "%s: dx overlaps x or d_y partially", fn);
   kda::LayerNormParams p{};
   if (dweight || dbias) {
     const size_t need = (size_t)kda::layer_norm_parts(rows, (int)D) * 2 * (size_t)D * sizeof(float);

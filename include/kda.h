@@ -472,7 +472,8 @@ int kda_gated_delta_backward(const void* q, const void* k, const void* v, kda_dt
  *
  * x [rows, D] of `dtype` (KDA_BF16 or KDA_F32), rows x_stride elements apart;
  * weight, bias [D] of `weight_dtype` (KDA_F32, or `dtype`), NULL for 1 and 0;
- * y [rows, D] contiguous, may be x itself where x is contiguous; mean, rstd
+ * y [rows, D] contiguous, may be x itself where x is contiguous (any other
+ * overlap is refused, here and of dx with its inputs); mean, rstd
  * [rows] fp32, kept for the backward pass. D in [1, 16384]. Any alignment of
  * whole elements is taken; rows on 16-byte boundaries are faster.
  *

@@ -101,6 +101,13 @@ int check_tensors(const char* fn, kda_dtype dtype, const Sizes& z, const kda_lay
   return KDA_OK;
 }
 
+// Rows of o on top of one another would be written by several blocks.
+int check_output(const char* fn, const Sizes& z, const kda::GatedDeltaParams& p) {
+  if ((z.B > 1 && p.os[0] == 0) || (z.T > 1 && p.os[1] == 0) || (z.HV > 1 && p.os[2] == 0))
+    return fail(KDA_ERR_INVALID_ARG, "%s: o has a stride of zero over an extent above one", fn);
+  return KDA_OK;
+}
+
 bool backward_dim(int64_t d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 
 // The workspace of a call; without `split`, the least that lets it run in chunks.
@@ -154,6 +161,7 @@ int kda_gated_delta_prefill(const void* q, const void* k, const void* v, kda_dty
   }
   kda::GatedDeltaParams p{};
   if (int rc = check_tensors(fn, dtype, z, layout, q, k, v, g, beta, o, p)) return rc;
+  if (int rc = check_output(fn, z, p)) return rc;
   p.s0 = initial_state;
   p.sf = final_state;
   p.cu = cu_seqlens;
@@ -177,6 +185,7 @@ int kda_gated_delta_decode_step(const void* q, const void* k, const void* v, kda
   if (!aligned16(state)) return fail(KDA_ERR_UNSUPPORTED, "%s: the state must be 16-byte aligned", fn);
   kda::GatedDeltaParams p{};
   if (int rc = check_tensors(fn, dtype, z, layout, q, k, v, g, beta, o, p)) return rc;
+  if (int rc = check_output(fn, z, p)) return rc;
   p.s0 = p.sf = state;
   p.N = (int)B;
   const cudaError_t e = kda::launch_gated_delta_decode(p, dtype, reinterpret_cast<cudaStream_t>(stream));

@@ -1,7 +1,10 @@
-"""Outputs that overlap an input in part are refused before a launch (no GPU needed)."""
+"""Outputs that overlap an input in part, or themselves, are refused before a launch (no GPU needed)."""
+import ctypes
+
 import pytest
 
 import gated_delta_rule_bounded_b200 as kda
+from gated_delta_rule_bounded_b200 import Layout, Strides
 
 OK, INVALID = 0, 1
 FAKE = 1 << 30  # a non-null, 16-byte aligned address that is never dereferenced
@@ -38,3 +41,15 @@ def test_norm_takes(lib, xs, y):
     """Refused for another reason, which is looked at later: a null pointer among the results."""
     assert lib.kda_layer_norm(FAKE, xs, kda.KDA_BF16, None, None, 1, 1e-5, ROWS, D, y, None, BIG, None) == INVALID
     assert "overlap" not in lib.kda_last_error().decode()
+
+
+@pytest.mark.parametrize("o", [(0, 512, 128), (8192, 0, 128), (8192, 512, 0)])
+def test_scan_refuses_outputs_over_one_another(lib, o):
+    s = (8192, 512, 128)
+    layout = Layout(*(Strides(*x) for x in ((4096, 256, 128), (4096, 256, 128), s, (64, 4, 1), (64, 4, 1), o)))
+    rc = lib.kda_gated_delta_prefill(FAKE, FAKE, FAKE, 1, FAKE, FAKE, None, None, None, 0, 2, 16, 2, 4, 128, 128,
+                                     ctypes.byref(layout), FAKE, None, 0, None)
+    assert rc == INVALID and "o " in lib.kda_last_error().decode()
+    if o[1]:
+        rc = lib.kda_gated_delta_decode_step(FAKE, FAKE, FAKE, 1, FAKE, FAKE, FAKE, 2, 2, 4, 128, 128, ctypes.byref(layout), FAKE, None)
+        assert rc == INVALID and "o " in lib.kda_last_error().decode()

@@ -13,7 +13,7 @@ functions raise if the library is missing or a tensor is not on a CUDA device.
 * :func:`decode_step` -- one token against a kept state, updated in place.
 * :func:`gated_delta_prefill`, :func:`gated_delta_decode_step`, :func:`gated_delta_backward` -- the gated
   delta rule with one decay per value head, and value heads that share query and key heads.
-* :func:`layer_norm`, :func:`layer_norm_backward` -- the norm that follows the scan.
+* :func:`layer_norm`, :func:`layer_norm_backward` -- layer norm over a head's output or a whole token.
 """
 from __future__ import annotations
 

@@ -17,7 +17,7 @@ struct QkMaps {
 // ---------------------------------------------------------------------------------------------------------------------
 // The length of a split's segments: which takes least time, counted in chunks of kernel S (2.6 us), when chains of at most
 // `longest` chunks run in waves over the SMs; a wave costs a chunk more to start, the launches 3, a joined segment 0.7.
-// Measured, 8 heads of 16,384 tokens: whole 657 us, estimated 668; in 19 segments 85 + 33 + 47 us, estimated 158.
+// Measured, 8 heads of 16,384 tokens: whole 667 us, estimated 668; in 19 segments 86 + 34 + 49 us, estimated 158.
 // ---------------------------------------------------------------------------------------------------------------------
 constexpr int SPLIT_LENGTHS = 31;
 __host__ __device__ inline int split_length(int least, int i) {  // the least times 2^(i / 4), about
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(32 * PACKED_WARPS) gated_delta_packed_kernel(G
 // steps too many for tcgen05's round trips; M and Z stand in shared memory as the two bf16 parts that are Z's images in
 // the end (Z written over M), so fragments come by ldmatrix, and Y turns from result to operand inside the registers
 // (movmatrix). The steps depend on one another, so what bounds the kernel is their latency until enough blocks share an
-// SM: five of 39 KB. Measured, 4096 tokens x 96 heads: 85 us for 358 MB (4.2 TB/s of 6.6; 256 threads and fp32 products
+// SM: five of 39 KB. Measured, 4096 tokens x 96 heads: 90 us for 358 MB (4.0 TB/s of 6.6; 256 threads and fp32 products
 // for the solves 152, mma.sync on eight warps 104).
 // ---------------------------------------------------------------------------------------------------------------------
 constexpr int P_THREADS = 128;

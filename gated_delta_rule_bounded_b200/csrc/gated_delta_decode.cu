@@ -7,7 +7,7 @@
 // partial sums meet in shared memory once, and the update needs no second read. Blocks are independent, and an SM holds
 // several, so one block's loads run under another's sums and stores. The tile is narrower where few heads would leave
 // SMs idle (VT = 32 gives four blocks for a 128-column head). Measured, 64 x 96 heads of 128 x 128 (805 MB of state both
-// ways): 120 us of kernel, 6.7 TB/s, what a copy reaches; 32 heads: 3 us of kernel in a call of 19 us.
+// ways): 125 us, 6.5 TB/s, what a copy reaches; 32 heads: 3.8 us of kernel in a call of 17 us.
 #include "common.cuh"
 #include "gated_delta.h"
 

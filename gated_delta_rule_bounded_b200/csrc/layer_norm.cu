@@ -1,5 +1,5 @@
-// layer_norm.cu -- layer norm over rows, forward and backward, as it follows the scan for every head (rows of V
-// values) or over a whole token (rows of H * V values).
+// layer_norm.cu -- layer norm over rows, forward and backward: of every head's output (rows of V values) or of a whole
+// token (rows of H * V values).
 //
 //   forward    mean = sum x / D,  rstd = 1 / sqrt(sum (x - mean)^2 / D + eps),  y = (x - mean) rstd w + b
 //   backward   with h = (x - mean) rstd and e = dy w:
@@ -20,12 +20,12 @@
 // workspace, and a second kernel adds the partial rows. The order of the sums depends on the sizes alone: the same
 // inputs give the same bits, with no atomics.
 //
-// Measured, bf16, L2 flushed before each call: 393,216 rows of 128 forward 42 us (4.8 TB/s of 6.6 a copy reaches),
-// backward 76 us (4.0 TB/s); 8,191 rows of 2,047 in fp32, pieces of one element, backward 57 us against 53 for 8,192
-// rows of 2,048; a call of 64 rows of 12,288 3.5 us of kernel. What bounds the backward pass of short rows is the eight
-// shuffles a row takes beside the accesses themselves (the load and store unit is busy 83 % of the time). Tried: eight
-// lanes a row with two pieces each, 88 us; rows staged by asynchronous copies four rounds ahead in shared memory, 74 us
-// here but 165 instead of 131 for rows of 4,096 (the slots' reads go through the same unit).
+// Measured, bf16, L2 flushed before each call: 393,216 rows of 128 forward 39 us (5.2 TB/s of 6.6 a copy reaches),
+// backward 70 us (4.4 TB/s), 4 of them for the sum of the partial rows; 8,191 rows of 2,047 in fp32, pieces of one element,
+// backward 51 us, the kernels 48 + 5 against 43 + 5 for 8,192 rows of 2,048; a call of 64 rows of 12,288 4.3 us of kernel.
+// In the backward pass of short rows nothing is saturated (L1 and shared memory 69 %, issue 59 %, DRAM 51 %): a warp waits
+// in turn on its loads and on the eight shuffles a row. Tried, when it took 76 us: eight lanes a row with two pieces each,
+// 88; rows staged by asynchronous copies four rounds ahead in shared memory, 74, but 165 instead of 131 for rows of 4,096.
 #include <algorithm>
 #include <atomic>
 

@@ -464,8 +464,8 @@ int kda_gated_delta_backward(const void* q, const void* k, const void* v, kda_dt
                              void* workspace, size_t workspace_bytes, kda_stream_t stream);
 
 /* ---------------------------------------------------------------------------
- * Layer norm over rows, as it follows the scan for every head (rows of V
- * values) or over a whole token.
+ * Layer norm over rows: of every head's output (rows of V values) or of whole
+ * tokens.
  *
  *   y = (x - mean) * rstd * weight + bias,  mean = sum x / D,
  *   rstd = 1 / sqrt(sum (x - mean)^2 / D + eps)

@@ -24,7 +24,7 @@ ROWS, D = 4, 64  # bf16: rows of 128 bytes
 @pytest.mark.parametrize("xs,y", [
     (64, FAKE + 128), (64, FAKE - 128), (64, FAKE + 2), (64, FAKE + 3 * 128 + 64),  # shifted by rows, by elements, the last half row
     (128, FAKE), (128, FAKE + 128), (0, FAKE), (32, FAKE),  # x is not contiguous: its rows are not y's
-    (512, FAKE + 1024 - 64), (512, FAKE + 3 * 1024 - 256),  # from between two rows into the next
+    (512, FAKE + 1024 - 64), (512, FAKE + 2 * 1024 - 256),  # from between two rows into the next
 ])
 def test_norm_refuses(lib, xs, y):
     assert lib.kda_layer_norm(FAKE, xs, kda.KDA_BF16, None, None, 1, 1e-5, ROWS, D, y, BIG, BIG + 4096, None) == INVALID
@@ -36,7 +36,7 @@ def test_norm_refuses(lib, xs, y):
 
 
 @pytest.mark.parametrize("xs,y", [(64, FAKE), (64, FAKE + 512), (64, FAKE - 512), (512, FAKE + 128), (512, FAKE + 1024 + 512),
-                                  (512, FAKE + 3 * 1024 + 128)])
+                                  (512, FAKE + 2 * 1024 + 128)])
 def test_norm_takes(lib, xs, y):
     """Refused for another reason, which is looked at later: a null pointer among the results."""
     assert lib.kda_layer_norm(FAKE, xs, kda.KDA_BF16, None, None, 1, 1e-5, ROWS, D, y, None, BIG, None) == INVALID
